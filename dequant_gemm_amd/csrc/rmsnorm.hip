@@ -20,16 +20,16 @@
 namespace nf4 {
 namespace {
 
-// Sum over the workgroup's TPB threads, in every thread.
-template <int TPB>
-__device__ __forceinline__ float block_sum(float v, float *lds) {
+// Sum over the workgroup's TPB threads, in every thread; S is float or double.
+template <int TPB, typename S>
+__device__ __forceinline__ S block_sum(S v, S *lds) {
   v = sum64(v);
   if (TPB == 64) return v;
   const int wave = threadIdx.x >> 6;
   __syncthreads();   // the previous use of lds is over
   if ((threadIdx.x & 63) == 0) lds[wave] = v;
   __syncthreads();
-  float s = lds[0];
+  S s = lds[0];
 #pragma unroll
   for (int i = 1; i < TPB / 64; ++i) s += lds[i];
   return s;
@@ -59,9 +59,10 @@ __device__ __forceinline__ void put_y(const float y[8], int64_t row, int64_t c, 
 // VPT == 0: any width, the row read twice.
 template <int TPB, int VPT, typename T, int OUT, bool VEC>
 __global__ __launch_bounds__(TPB) void rmsnorm_fwd_kernel(RowsIn x, RowsIn res, const void *w, bool w_bf16,
-                                                          int64_t rows, int64_t cols, float eps, T *__restrict__ h,
-                                                          void *__restrict__ y, Fp8Out q, float *__restrict__ rstd) {
-  __shared__ float lds[TPB / 64];
+                                                          int64_t rows, int64_t cols, double inv_cols, float eps,
+                                                          T *__restrict__ h, void *__restrict__ y, Fp8Out q,
+                                                          float *__restrict__ rstd) {
+  __shared__ double lds[TPB / 64];
   const int64_t row = group_number();
   if (row >= rows) return;
   const T *xr = reinterpret_cast<const T *>(x.p) + row * x.ld;
@@ -90,8 +91,9 @@ __global__ __launch_bounds__(TPB) void rmsnorm_fwd_kernel(RowsIn x, RowsIn res, 
   } else {
     for (int64_t c = c0; c < cols; c += STEP) take(c, v[0]);
   }
-  sum = block_sum<TPB>(sum, lds);
-  const float rs = 1.f / sqrtf(sum / (float)cols + eps);
+  // A row's scalar: one rounding, where the sum over lanes, the mean, the root and the quotient in fp32 would
+  // be ten (the mean square of its error 0.33 of a step and 0.60; an e4m3 code near a tie falls by it).
+  const float rs = (float)rsqrt(block_sum<TPB>((double)sum, lds) * inv_cols + (double)eps);
   if (threadIdx.x == 0) rstd[row] = rs;
 
   auto give = [&](int64_t c, const float e[8]) {
@@ -277,10 +279,10 @@ void fwd_vec(bool vec, RowsIn x, RowsIn res, const void *w, bool w_bf16, int64_t
   const dim3 g = grid_of(rows), b(TPB);
   if (vec)
     hipLaunchKernelGGL((rmsnorm_fwd_kernel<TPB, VPT, T, OUT, true>), g, b, 0, s, x, res, w, w_bf16, rows, cols,
-                       eps, reinterpret_cast<T *>(h), y, q, rstd);
+                       1.0 / (double)cols, eps, reinterpret_cast<T *>(h), y, q, rstd);
   else
     hipLaunchKernelGGL((rmsnorm_fwd_kernel<TPB, VPT, T, OUT, false>), g, b, 0, s, x, res, w, w_bf16, rows, cols,
-                       eps, reinterpret_cast<T *>(h), y, q, rstd);
+                       1.0 / (double)cols, eps, reinterpret_cast<T *>(h), y, q, rstd);
 }
 
 template <typename T, int OUT>

@@ -1,0 +1,49 @@
+"""GPU: the RMS norm where its roundings, its padding and its gradient's sums can go wrong."""
+import pytest
+import torch
+
+from tests import _ops_oracle as R
+from tests._gpu import dev, lib, note
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _randn(*shape, seed, std=1.0, dtype=F32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype)
+
+
+@pytest.mark.parametrize("H", [64, 512, 1000, 4096, 8192, 16384, 20000])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_rstd_is_rounded_about_once(H, dt):
+    """A correctly rounded rstd is off by a uniform half step, 0.29 of a step in the mean square; the fp32
+    additions of a thread's own squares (24 at most, averaged over the threads) leave it under 0.4."""
+    dg, d = lib(), dev()
+    note(f"rmsnorm: rstd of 2000 x {H} {dt}")
+    x = _randn(2000, H, seed=H, std=2.0) * torch.linspace(0.5, 4.0, 2000)[:, None]
+    x = x.to(dt)
+    _, _, rstd = dg.nf4_rmsnorm_fwd(x.to(d), torch.ones(H, device=d), eps=2.0 ** -20)
+    torch.cuda.synchronize()
+    ref = 1.0 / torch.sqrt((x.double() ** 2).mean(1) + 2.0 ** -20)
+    step = torch.exp2(torch.floor(torch.log2(ref)) - 23)
+    off = float((((rstd.cpu().double() - ref) / step) ** 2).mean().sqrt())
+    assert off < 0.4, off
+
+
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -149, 1e-30, 1e30])
+def test_rstd_of_extreme_rows(eps):
+    dg, d = lib(), dev()
+    note(f"rmsnorm: extreme rows, eps {eps}")
+    x = torch.zeros(5, 24)
+    x[1], x[2], x[3], x[4] = 1e-18, 1e18, 2.0 ** -75, 3e38
+    _, _, rstd = dg.nf4_rmsnorm_fwd(x.to(d), torch.ones(24, device=d), eps=eps)
+    torch.cuda.synchronize()
+    s = (x * x).sum(1).double() / 24 + torch.tensor(eps, dtype=F32).double()     # the squares are fp32's
+    ref = (1.0 / torch.sqrt(s)).float()
+    got = rstd.cpu()
+    assert torch.equal(got.isinf(), ref.isinf()) and not got.isnan().any()
+    ok = ref.isfinite()
+    # a thread's seven additions of equal squares, halved by the root, and one rounding
+    assert ((got - ref).abs()[ok] <= ref[ok] * 5 * R.EPS32).all()
