@@ -92,7 +92,7 @@ __global__ __launch_bounds__(TPB) void rmsnorm_fwd_kernel(RowsIn x, RowsIn res, 
     for (int64_t c = c0; c < cols; c += STEP) take(c, v[0]);
   }
   // A row's scalar: one rounding, where the sum over lanes, the mean, the root and the quotient in fp32 would
-  // be ten (the mean square of its error 0.33 of a step and 0.60; an e4m3 code near a tie falls by it).
+  // be ten (the root mean square of its error 0.30 of a step, and 0.5 to 0.6; e4m3 codes near a tie fall by it).
   const float rs = (float)rsqrt(block_sum<TPB>((double)sum, lds) * inv_cols + (double)eps);
   if (threadIdx.x == 0) rstd[row] = rs;
 
@@ -101,6 +101,10 @@ __global__ __launch_bounds__(TPB) void rmsnorm_fwd_kernel(RowsIn x, RowsIn res, 
     load_part<VEC>(w, w_bf16, c, cols, g);
 #pragma unroll
     for (int k = 0; k < 8; ++k) o[k] = e[k] * rs * g[k];
+    if (OUT == kOutFp8 && c + 8 > cols) {   // the padding is zeros, also of a row whose rs is not finite
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = c + k < cols ? o[k] : 0.f;
+    }
     put_y<OUT, VEC>(o, row, c, cols, y, q);
   };
   if (VPT) {

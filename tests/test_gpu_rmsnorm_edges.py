@@ -47,3 +47,26 @@ def test_rstd_of_extreme_rows(eps):
     ok = ref.isfinite()
     # a thread's seven additions of equal squares, halved by the root, and one rounding
     assert ((got - ref).abs()[ok] <= ref[ok] * 5 * R.EPS32).all()
+
+
+@pytest.mark.parametrize("H", [1, 100, 260, 300, 1100, 5001, 20100])
+@pytest.mark.parametrize("dt,res", [(BF, False), (F32, True)])
+def test_padding_of_rows_without_a_norm(H, dt, res):
+    """Codes and scales past the row's end are zeros, also where rstd is NaN, infinite or zero."""
+    dg, d = lib(), dev()
+    note(f"rmsnorm fp8: padding of {H} {dt} res={res}")
+    x = _randn(5, H, seed=H, dtype=dt)
+    x[0, H // 2] = float("nan")
+    x[1] = 0
+    x[2, 0] = float("inf")
+    r = torch.zeros_like(x) if res else None
+    w = torch.ones(H)
+    q, _, _ = dg.nf4_rmsnorm_fwd_fp8(x.to(d), w.to(d), None if r is None else r.to(d), eps=0.0)
+    good, _, _ = dg.nf4_rmsnorm_fwd_fp8(x[3:].to(d), w.to(d), None if r is None else r[3:].to(d), eps=0.0)
+    torch.cuda.synchronize()
+    codes = q.data.cpu().view(torch.uint8)
+    assert (codes[:, H:] == 0).all()
+    assert (q.scale.cpu()[:, -(-H // 128):] == 0).all()
+    v = q.dequantize().cpu()
+    assert v[:2].isnan().all() and bool(v[2, 0].isnan())
+    assert torch.equal(codes[3:], good.data.cpu().view(torch.uint8)) and torch.equal(q.scale[3:], good.scale)
