@@ -4,7 +4,9 @@ The optimizer of what is trained beside frozen quantized weights: adapters and
 norm weights ("bitsandbytes" page: 8-bit optimizer states).  ``state_bits=8``
 holds the first moment and the root of the second in e4m3 with an fp32 scale per
 256 elements, rounded at random without bias (2.03 bytes of state an element;
-fp32 8).
+fp32 8).  A code reaches down to 4e-6 of its block's largest value: elements
+whose gradients stay below that beside their neighbours' take shorter steps than
+with fp32 moments, since their root is held at the smallest code.
 """
 from __future__ import annotations
 

@@ -458,7 +458,9 @@ int nf4_adamw_layout(const int64_t *n, int64_t count, void *out, size_t bytes);
  * x *= 0x983B6369; x ^= x >> 15; x *= 0xC1F49415; x ^= x >> 16 } and the key
  * mix(number of the tensor + seed), element i takes mix(i + key) (for
  * i >= 2^32 the key is mix(key + (i >> 32) 0x11D5D725)), the low half for the
- * first moment, the high half for the second.  Non-finite moments become NaN
+ * first moment, the high half for the second.  A root that is not zero takes at
+ * least the smallest code (2^-9 of the scale): a step never divides a moment by
+ * a root that rounding took away.  Non-finite moments become NaN
  * codes and do not enter their block's scale.  `tensors` (host, `count`
  * entries) is read during the call only; entries with n == 0 are passed over.
  * Tensors must not overlap.  With config->layout the states of all `count`
