@@ -11,12 +11,14 @@ As in ``nn``: the quantized weight is frozen and gets no gradient ("bitsandbytes
 page, 4-bit/LoRA paragraph: frozen quantized base weights with trainable
 parameters beside them); inputs are bf16 or fp32 of any leading shape; no bias.
 Quantization of activations counts as the identity in the backward pass.
+Gradients are of first order: a derivative of one (``create_graph=True``) raises.
 """
 from __future__ import annotations
 
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._ops import (FP8_FORMATS, FP8Tensor, nf4_fp8_matmul, nf4_fp8_quantize, nf4_rmsnorm_bwd, nf4_rmsnorm_fwd,
                    nf4_rmsnorm_fwd_fp8)
@@ -52,6 +54,7 @@ class _RMSNorm(torch.autograd.Function):
         return (y, h.reshape(x.shape)) if ctx.has_residual else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy, gh=None):
         h, weight, rstd = ctx.saved_tensors
         H = weight.shape[0]
@@ -96,6 +99,7 @@ class _FP8Linear(torch.autograd.Function):
         return y.reshape(*x.shape[:-1], w.rows)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         return _input_gradient(gy, ctx.wt, ctx.fmt, ctx.dtype).reshape(ctx.shape), None, None, None, None
 
@@ -175,6 +179,7 @@ class _FP8NormLinear(torch.autograd.Function):
         return (y, h.reshape(x.shape)) if ctx.has_residual else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy, gh=None):
         h, weight, rstd = ctx.saved_tensors
         dn = _input_gradient(gy, ctx.wt, ctx.fmt, torch.bfloat16)      # of the norm's output
