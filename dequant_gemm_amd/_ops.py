@@ -14,7 +14,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from ._lib import AdamWTensorStruct, FP8TensorStruct, _check, _dtype_enum, _require_device, _stream, lib
+from ._lib import AdamWTensorStruct, FP8TensorStruct, _check, _dtype_enum, _require_device, lib
 
 FP8_BLOCK = 128          # columns (and, for weights, rows) per scale
 ADAM_BLOCK = 256         # elements per scale of an 8-bit optimizer state
@@ -152,18 +152,13 @@ def nf4_fp8_quantize(x: torch.Tensor, block_rows: int = 1, fmt: str = "e4m3",
     """8-bit codes of a 2-D bf16/fp32 device tensor with contiguous rows: activations (``block_rows`` 1)
     or weights (128).  ``out``: buffers to fill (their ``block_rows`` and type then hold)."""
     if out is not None:
-        if out.device != x.device or out.shape != tuple(x.shape):
-            raise ValueError(f"out is {out.shape} on {out.device}, x {tuple(x.shape)} on {x.device}")
-        if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-            raise ValueError("x must be 2-D with contiguous rows")
-        ld = max(x.stride(0) if x.shape[0] > 1 else x.shape[1], 1)
-        st = out.struct()
-        _check(lib().nf4_fp8_quantize(x.data_ptr(), _dtype_enum(x.dtype), ld, ctypes.byref(st), _stream(x.device)),
-               "nf4_fp8_quantize")
+        if out.shape != tuple(x.shape):
+            raise ValueError(f"out is {out.shape}, x {tuple(x.shape)}")
+        _status(_host().fp8_quantize(x, out.block_rows, 0, _raw_stream(x), out.data, out.scale), "nf4_fp8_quantize")
         return out
     if fmt not in FP8_FORMATS:
         raise ValueError(f"fmt must be one of {tuple(FP8_FORMATS)} (got {fmt!r})")
-    data, scale = _status(_host().fp8_quantize(x, block_rows, 1 if fmt == "e5m2" else 0, _raw_stream(x)),
+    data, scale = _status(_host().fp8_quantize(x, block_rows, 1 if fmt == "e5m2" else 0, _raw_stream(x), None, None),
                           "nf4_fp8_quantize")
     return FP8Tensor(x.shape[0], x.shape[1], block_rows, data, scale)
 

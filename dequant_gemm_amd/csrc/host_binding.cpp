@@ -273,14 +273,21 @@ PyObject *do_rmsnorm_bwd(PyObject *const *a, Py_ssize_t n) {
   return st ? PyLong_FromLong(st) : tuple_of({dx, dw});
 }
 
-// fp8_quantize(x, block_rows, format, stream) -> (data, scale)
+// fp8_quantize(x, block_rows, format, stream, data | None, scale | None) -> (data, scale); given, they are filled
 PyObject *do_fp8_quantize(PyObject *const *a, Py_ssize_t n) {
-  count_args(n, 4);
+  count_args(n, 6);
   const Tensor &x = tensor(a[0], "x");
   const int64_t ld = matrix(x, "x"), block_rows = integer(a[1]), format = integer(a[2]);
   if (block_rows != 1 && block_rows != NF4_FP8_BLOCK) throw BadValue{"block_rows must be 1 or 128"};
   const c10::DeviceGuard guard(x.device());
   if (x.size(1) < 1) throw BadValue{"an 8-bit tensor needs at least one column"};
+  if (a[4] != Py_None) {
+    const Tensor &data = tensor(a[4], "out.data"), &scale = tensor(a[5], "out.scale");
+    const nf4_fp8_tensor q = fp8_of(x.size(0), x.size(1), block_rows, data, scale, "out");
+    same_place(data, x, "out");
+    const int st = nf4_fp8_quantize(x.data_ptr(), dtype_enum(x, "x"), ld, &q, pointer(a[3]));
+    return st ? PyLong_FromLong(st) : tuple_of({data, scale});
+  }
   Outputs o(x);
   add_fp8(o, x.size(0), x.size(1), block_rows, (int)format);
   o.allocate();
