@@ -168,6 +168,11 @@ nf4_fp8_tensor fp8_of(int64_t rows, int64_t cols, int64_t block_rows, const Tens
                         (float *)scale.data_ptr()};
 }
 
+// Tells autograd that a caller's tensor was written: a backward pass that saved it then raises.
+void written(const Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();   // (an inference tensor counts none)
+}
+
 int64_t integer(PyObject *o) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw python_error();
@@ -286,7 +291,10 @@ PyObject *do_fp8_quantize(PyObject *const *a, Py_ssize_t n) {
     const nf4_fp8_tensor q = fp8_of(x.size(0), x.size(1), block_rows, data, scale, "out");
     same_place(data, x, "out");
     const int st = nf4_fp8_quantize(x.data_ptr(), dtype_enum(x, "x"), ld, &q, pointer(a[3]));
-    return st ? PyLong_FromLong(st) : tuple_of({data, scale});
+    if (st) return PyLong_FromLong(st);
+    written(data);
+    written(scale);
+    return tuple_of({data, scale});
   }
   Outputs o(x);
   add_fp8(o, x.size(0), x.size(1), block_rows, (int)format);
@@ -319,7 +327,9 @@ PyObject *do_fp8_matmul(PyObject *const *a, Py_ssize_t n) {
     y = fresh(xd, {x.rows, w.rows}, integer(a[11]) == NF4_BF16 ? at::kBFloat16 : at::kFloat);
   }
   const int st = nf4_fp8_matmul(&x, &w, y.data_ptr(), dtype_enum(y, "out"), pointer(a[12]));
-  return st ? PyLong_FromLong(st) : THPVariable_Wrap(y);
+  if (st) return PyLong_FromLong(st);
+  if (a[10] != Py_None) written(y);
+  return THPVariable_Wrap(y);
 }
 
 // adamw_step(params, grads, descriptors, count, device index, lr, beta1, beta2, eps, weight_decay, step,
@@ -372,7 +382,10 @@ PyObject *do_adamw_step(PyObject *const *a, Py_ssize_t n) {
   c.param_dtype = types[0];
   c.grad_dtype = types[1];
   const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
-  return PyLong_FromLong(nf4_adamw_step(d, count, &c, pointer(a[15])));
+  const int st = nf4_adamw_step(d, count, &c, pointer(a[15]));
+  if (!st)
+    for (int64_t i = 0; i < count; ++i) written(THPVariable_Unpack(PySequence_Fast_GET_ITEM(ps.get(), i)));
+  return PyLong_FromLong(st);
 }
 
 template <PyObject *(*F)(PyObject *const *, Py_ssize_t)>
