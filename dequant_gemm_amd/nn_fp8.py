@@ -182,7 +182,7 @@ class _FP8NormLinear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gy, gh=None):
         h, weight, rstd = ctx.saved_tensors
-        dn = _input_gradient(gy, ctx.wt, ctx.fmt, torch.bfloat16)      # of the norm's output
+        dn = _input_gradient(gy, ctx.wt, ctx.fmt, h.dtype)             # of the norm's output
         dx, dw = nf4_rmsnorm_bwd(dn, h, weight, rstd, None if gh is None else _rows(gh, h.shape[1]))
         dx = dx.reshape(ctx.shape)
         return dx, dw, dx if ctx.has_residual else None, None, None, None, None, None

@@ -77,3 +77,15 @@ def test_first_derivatives_of_the_norm(plain):
     xr, wr = x.detach().double().requires_grad_(), w.detach().double().requires_grad_()
     (xr * ((xr ** 2).mean(1, keepdim=True) + 1e-3).rsqrt() * wr).backward(torch.full((4, 6), 0.3).double())
     assert torch.allclose(x.grad.double(), xr.grad, atol=1e-6) and torch.allclose(w.grad.double(), wr.grad, atol=1e-6)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_the_norms_gradient_keeps_the_streams_type(plain, dt):
+    """The gradient between the product and the norm is formed in x's type, as the two layers apart form it."""
+    q = FP8Tensor.from_parts(torch.ones(5, 7).to(torch.float8_e4m3fn), torch.ones(1, 1), 128)
+    layer = nn_fp8.FP8NormLinear(q, norm_dtype=torch.float32, out_dtype=torch.float32)
+    x = torch.randn(3, 7).to(dt).requires_grad_()
+    y = layer(x)
+    del plain[:]
+    y.sum().backward()
+    assert plain == [dt] and x.grad.dtype == dt
