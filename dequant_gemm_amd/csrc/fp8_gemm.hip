@@ -137,7 +137,8 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_small_kernel(Fp8In x, Fp8In w,
   __shared__ f32x4 part[WAVES][NR][MT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * NR), m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int64_t n0 = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * (16 * NR), m0 = (int64_t)blockIdx.y * (16 * MT);
+  if (n0 >= w.rows) return;   // past the last of a grid of several layers
   const int KB = (int)(w.pitch / kFp8Block);
   const uint8_t *wp[NR], *xp[MT];
   const float *sw[NR], *sx[MT];
@@ -273,7 +274,9 @@ void fp8_tile_kernel(Fp8In x, Fp8In w, void *__restrict__ y, int tiles_n, int ti
   const int total = tiles_n * tiles_m;
   int t;
   {
-    const int q = total / 8, rem = total % 8, xcd = blockIdx.x % 8, idx = blockIdx.x / 8;
+    const int group = (int)group_number();      // (a row of the grid is a multiple of 8 workgroups)
+    if (group >= total) return;
+    const int q = total / 8, rem = total % 8, xcd = group % 8, idx = group / 8;
     t = xcd * q + (xcd < rem ? xcd : rem) + idx;
   }
   int tn, tm;
@@ -463,13 +466,14 @@ template <int WN, int WM, int KS, int TN, int TM, bool E5M2, bool F32OUT, bool V
 void launch_tile(const Fp8In &x, const Fp8In &w, void *y, hipStream_t s) {
   constexpr int BN = 16 * TN * WN, BM = 16 * TM * WM;
   const int tn = (int)((w.rows + BN - 1) / BN), tm = (int)((x.rows + BM - 1) / BM);
-  hipLaunchKernelGGL((fp8_tile_kernel<WN, WM, KS, TN, TM, E5M2, F32OUT, VEC>), dim3((unsigned)(tn * tm)),
+  hipLaunchKernelGGL((fp8_tile_kernel<WN, WM, KS, TN, TM, E5M2, F32OUT, VEC>), grid_of((int64_t)tn * tm),
                      dim3(64 * WN * WM * KS), 0, s, x, w, y, tn, tm);
 }
 
 template <int MT, int NR, int U, int WAVES, bool E5M2, bool F32OUT, bool VEC>
 void launch_small(const Fp8In &x, const Fp8In &w, void *y, hipStream_t s) {
-  const dim3 g((unsigned)((w.rows + 16 * NR - 1) / (16 * NR)), (unsigned)((x.rows + 16 * MT - 1) / (16 * MT)));
+  const dim3 n = grid_of((w.rows + 16 * NR - 1) / (16 * NR));
+  const dim3 g(n.x, (unsigned)((x.rows + 16 * MT - 1) / (16 * MT)), n.y);
   hipLaunchKernelGGL((fp8_small_kernel<MT, NR, U, WAVES, E5M2, F32OUT, VEC>), g, dim3(64 * WAVES), 0, s, x, w, y);
 }
 
@@ -604,8 +608,7 @@ void launch_out(const Fp8In &x, const Fp8In &w, void *y, bool y_bf16, hipStream_
 }  // namespace
 
 bool fp8_matmul_fits(int64_t M, int64_t N) {
-  // a tile's number, and eight rows of tiles, stay below 2^31 at 64 x 64, and
-  // the small kernels' 1024 threads per 16 rows of W below 2^32
+  // a tile's number, and eight rows of tiles, stay below 2^31 at 64 x 64
   return N < ((int64_t)1 << 26) && (M + 63) / 64 <= ((int64_t)1 << 31) / 8 / ((N + 63) / 64);
 }
 

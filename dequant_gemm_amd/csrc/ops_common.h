@@ -290,8 +290,9 @@ __device__ __forceinline__ float amax8(const float v[8]) {
 
 // ------------------------------------------------------------------ launchers
 
-// A grid for `n` workgroups numbered by group_number(): a launch holds fewer than
-// 2^32 threads along x, which many short rows would pass.
+// A grid for `n` workgroups of up to 1024 threads numbered by group_number(): a
+// launch holds fewer than 2^32 threads along x, which many short rows or small
+// tiles would pass.  Workgroups past n leave at once.
 inline dim3 grid_of(int64_t n) {
   constexpr int64_t kX = (int64_t)1 << 21;
   return n <= kX ? dim3((unsigned)n) : dim3((unsigned)kX, (unsigned)((n + kX - 1) / kX));
