@@ -47,6 +47,14 @@ class AdamW(torch.optim.Optimizer):
         for group in self.param_groups:
             self._check(group)
 
+    def __getstate__(self):
+        return {**super().__getstate__(), "state_bits": self.state_bits, "seed": self.seed, "calls": self.calls}
+
+    def __setstate__(self, state):
+        """A copy or a loaded pickle: its buckets are built anew, with the moments that came with the parameters."""
+        super().__setstate__(state)
+        self._buckets = [{} for _ in self.param_groups]
+
     def add_param_group(self, group):
         super().add_param_group(group)
         if hasattr(self, "_buckets"):
@@ -75,13 +83,30 @@ class AdamW(torch.optim.Optimizer):
         return b.values()
 
     def _expose(self, bucket: _Bucket, i: int, p):
-        """The parameter's share of the flat buffers, as torch keeps optimizer state (for state_dict)."""
+        """The parameter's share of the flat buffers, as torch keeps optimizer state (for state_dict).
+
+        State that is there already (in a copy of the optimizer) is taken over.
+        """
         st = bucket.state
         lo, hi = st.starts[i], st.starts[i] + -(-st.sizes[i] // 256) * 256
         d = {"step": bucket.steps[i], "exp_avg": st.m[lo:hi], "exp_avg_sq": st.v[lo:hi]}
         if st.bits == 8:
             d["exp_avg_scale"], d["exp_avg_sq_scale"] = st.m_scale[lo // 256:hi // 256], st.v_scale[lo // 256:hi // 256]
+        if self.state.get(p):
+            self._take(bucket, i, d, self.state[p])
         self.state[p] = d
+
+    @staticmethod
+    def _take(bucket: _Bucket, i: int, d, src):
+        """Copies the state `src` of a parameter into its share `d` of the buffers."""
+        for k, t in d.items():
+            if k == "step":
+                continue
+            if src[k].shape != t.shape or src[k].dtype != t.dtype:
+                raise ValueError(f"saved {k} is {tuple(src[k].shape)} {src[k].dtype}, expected "
+                                 f"{tuple(t.shape)} {t.dtype}")
+            t.view(torch.uint8).copy_(src[k].view(torch.uint8))
+        bucket.steps[i] = d["step"] = int(src["step"])
 
     @torch.no_grad()
     def step(self, closure=None, grad_scale: Optional[torch.Tensor] = None):
@@ -138,11 +163,4 @@ class AdamW(torch.optim.Optimizer):
                                 t.view(torch.uint8).zero_()
                         b.steps[i] = self.state[p]["step"] = 0
                         continue
-                    for k, t in self.state[p].items():
-                        if k == "step":
-                            continue
-                        if src[k].shape != t.shape or src[k].dtype != t.dtype:
-                            raise ValueError(f"saved {k} is {tuple(src[k].shape)} {src[k].dtype}, expected "
-                                             f"{tuple(t.shape)} {t.dtype}")
-                        t.view(torch.uint8).copy_(src[k].view(torch.uint8))
-                    b.steps[i] = self.state[p]["step"] = int(src["step"])
+                    self._take(b, i, self.state[p], src)
