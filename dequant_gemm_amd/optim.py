@@ -58,7 +58,11 @@ class AdamW(torch.optim.Optimizer):
     def add_param_group(self, group):
         super().add_param_group(group)
         if hasattr(self, "_buckets"):
-            self._check(self.param_groups[-1])
+            try:
+                self._check(self.param_groups[-1])
+            except (TypeError, ValueError):
+                self.param_groups.pop()
+                raise
             self._buckets.append({})
 
     @staticmethod

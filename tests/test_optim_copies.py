@@ -1,4 +1,4 @@
-"""CPU: copies of the optimizer (its step needs a GPU, its state does not)."""
+"""CPU: copies of the optimizer, and parameter groups it refuses (its step needs a GPU, its state does not)."""
 import copy
 import io
 
@@ -61,3 +61,15 @@ def test_a_copy_made_before_the_first_step():
     p = torch.nn.Parameter(torch.zeros(3))
     other = copy.deepcopy(dg.AdamW([p], state_bits=8))
     assert all(not m.any() for x in _moments(other) for m in x)
+
+
+def test_a_refused_group_is_not_added():
+    p = torch.nn.Parameter(torch.zeros(3))
+    opt = dg.AdamW([p])
+    for bad, kind in ((torch.zeros(3, dtype=torch.float16), TypeError), (torch.zeros(4, 3).t(), ValueError)):
+        with pytest.raises(kind):
+            opt.add_param_group({"params": [torch.nn.Parameter(bad)]})
+        assert len(opt.param_groups) == 1 and len(opt._buckets) == 1
+    q = torch.nn.Parameter(torch.ones(2))
+    opt.add_param_group({"params": q, "lr": 0.5})
+    assert len(opt._buckets) == 2 and [list(b.params) for b in opt._buckets_of(1)] == [[q]]
