@@ -102,7 +102,11 @@ def _run(cmd):
 
 def build(asm_dir: str | None = None, verbose: bool = True) -> str:
     """Compiles every source and links libnf4.so (and the benchmark's libnf4_bench.so and the
-    binding's _host.so); returns the path of libnf4.so."""
+    binding's _host.so); returns the path of libnf4.so.
+
+    _host.so needs g++ and the headers of Python and torch, the libraries hipcc alone: they are
+    in place when a failure of _host.so is raised.
+    """
     lib = LIB
     os.makedirs(OBJDIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES + BENCH_SOURCES), os.cpu_count() or 1)) as ex:
@@ -112,9 +116,13 @@ def build(asm_dir: str | None = None, verbose: bool = True) -> str:
         tmp = out + ".tmp"
         _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *part])
         os.replace(tmp, out)
-    _link_host(host.result())
     if verbose:
         print(f"built {lib}")
+    try:
+        _link_host(host.result())
+    except Exception as e:
+        raise RuntimeError(f"the Python module {HOST_LIB} (the operators around the linear layers, _host) was not "
+                           f"built; the C library {lib} (libnf4) was: {e}") from e
     return lib
 
 
