@@ -1,4 +1,4 @@
-"""GPU: 8-bit moments of gradients that differ by many binades within a block."""
+"""GPU: 8-bit moments of gradients that differ by many binades within a block, and of a very long tensor."""
 import pytest
 import torch
 
@@ -7,6 +7,8 @@ from tests import _ops_oracle as R
 from tests._gpu import dev, lib, note
 
 pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
 
 
 def _mixed(n, outlier, rest, seed):
@@ -46,3 +48,28 @@ def test_codes_beside_an_outlier():
     assert (got[5:40] == 0).all() and (got[:5] > 0).all() and (got[n:] == 0).all()
     want, _ = R.encode_state(m, h & 0xFFFF)
     assert int((st.m.cpu().float().double() != want).sum()) <= 1
+
+
+def test_8bit_element_indexes_past_32_bits():
+    """Past element 2^32 the random bits take the key that holds the index's high half."""
+    dg, d = lib(), dev()
+    note("adamw 8-bit: 2^32 + 1000 elements")
+    n, tail = (1 << 32) + 1000, 1000
+    k = {"lr": 1e-3, "beta1": 0.9, "beta2": 0.999, "eps": 1e-8, "weight_decay": 0.0}
+    p, g = torch.zeros(n, dtype=BF, device=d), torch.zeros(n, dtype=BF, device=d)
+    gt = (torch.randn(tail, generator=torch.Generator().manual_seed(3)) * 1e-2).to(BF)
+    g[-tail:] = gt.to(d)
+    st = dg.AdamWState([n], 8, d)
+    dg.nf4_adamw_step([p], [g], st, step=1, seed=77, **k)
+    torch.cuda.synchronize()
+    _, m, v = R.adamw(torch.zeros(tail), gt, torch.zeros(tail), torch.zeros(tail), {**k, "step": 1})
+    key = R.mix((R.mix(77) + 0x11D5D725) & 0xFFFFFFFF)
+    h = R.mix((torch.arange(tail, dtype=torch.int64) + key) & 0xFFFFFFFF)
+    lo = 1 << 32
+    want, _ = R.encode_state(m, h & 0xFFFF)
+    assert int((st.m[lo:].cpu().float().double() != want).sum()) <= 1
+    want, _ = A.encode_root(v.sqrt(), h >> 16)
+    assert int((st.v[lo:].cpu().float().double() != want).sum()) <= 1
+    assert not st.m[:lo].view(torch.int64).any() and not st.v[:lo].view(torch.int64).any()
+    del st, p, g
+    torch.cuda.empty_cache()

@@ -70,3 +70,26 @@ def test_padding_of_rows_without_a_norm(H, dt, res):
     v = q.dequantize().cpu()
     assert v[:2].isnan().all() and bool(v[2, 0].isnan())
     assert torch.equal(codes[3:], good.data.cpu().view(torch.uint8)) and torch.equal(q.scale[3:], good.scale)
+
+
+# dense rows: several to a workgroup of one wave and of many, the kernel for rows wider than the registers
+# with more than one row a workgroup, and the doubled workgroups of odd widths
+@pytest.mark.parametrize("T,H", [(600, 16392), (600, 16401), (1111, 5001), (2100, 1000), (9000, 1123), (9000, 333),
+                                 (700, 12000), (1200, 6001), (5000, 64)])
+@pytest.mark.parametrize("xt,dt,wt,res", [(BF, BF, BF, True), (F32, BF, F32, False)])
+def test_gradient_of_many_dense_rows(T, H, xt, dt, wt, res):
+    dg, d = lib(), dev()
+    note(f"rmsnorm bwd {T}x{H} h {xt} dy {dt} dh={res}")
+    h, dy = _randn(T, H, seed=1, std=2.0, dtype=xt), _randn(T, H, seed=2, std=0.1, dtype=dt)
+    w = (1 + _randn(H, seed=3, std=0.2)).to(wt)
+    dh = _randn(T, H, seed=4, dtype=xt) if res else None
+    rstd = (1 / torch.sqrt((h.double() ** 2).mean(1) + 1e-5)).float()
+    dx, dw = dg.nf4_rmsnorm_bwd(dy.to(d), h.to(d), w.to(d), rstd.to(d), None if dh is None else dh.to(d))
+    torch.cuda.synchronize()
+    rx, rw, mx, mw = R.rmsnorm_grad(dy, h, w, rstd, dh)
+    # dx: under 64 additions of a thread, the lanes and the waves, and a few products;
+    # dw: at most 36 rows of a workgroup, 4096 / 64 of a lane, 63 lanes and two products
+    for name, got, ref, mag, n in (("dx", dx, rx, mx, 128), ("dw", dw, rw, mw, 192)):
+        err = (got.cpu().double() - ref).abs()
+        tol = n * R.EPS32 * mag + R.half_step(got.dtype) * 1.01 * ref.abs() + 1e-300
+        assert (err <= tol).all(), f"{name}: worst {float((err / tol).max()):.3f} of the bound"
