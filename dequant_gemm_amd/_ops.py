@@ -168,7 +168,9 @@ def nf4_fp8_matmul(x: FP8Tensor, w: FP8Tensor, out_dtype: torch.dtype = torch.fl
     """Y = X W^T of an 8-bit activation [M, K] and an 8-bit weight [N, K] (e4m3), fp32 accumulation.
 
     ``out_dtype`` float32 adds every product in fp32; bfloat16 runs on the fp8
-    matrix cores, whose sums are good to about 1e-5 before the rounding.
+    matrix cores, whose sums are good to about 1e-5 before the rounding.  A
+    block's two scales are multiplied first: their product should stay below
+    2^128, and below 2^-126 its rounding is worth up to 2^-118 of Y.
     """
     return _status(_host().fp8_matmul(x.rows, x.cols, x.block_rows, x.data, x.scale, w.rows, w.cols, w.block_rows,
                                       w.data, w.scale, out, _dtype_enum(out_dtype), _raw_stream(x.data)),

@@ -21,7 +21,7 @@
 // Non-finite moments take no part in a block's scale and become NaN codes.
 //
 // One pass over the tensors, HBM bound (45 million bf16 parameters: fp32 states
-// 193 us, 5.1 TB/s; 8-bit states 74 us, 6.1 TB/s).  Tensor descriptors travel as
+// 192 us, 5.2 TB/s; 8-bit states 88 us, 5.1 TB/s).  Tensor descriptors travel as
 // kernel arguments, as many as 4 KiB hold per launch: whole ones (Batch), or for a
 // state in flat buffers the parameters' and gradients' addresses (Flat).
 #include "nf4.h"
@@ -105,9 +105,10 @@ struct Batch {
 
 // The same for a state in flat buffers: where its tensors lie is in its owner's
 // layout, and a launch carries two offsets a tensor.  One launch then takes 448
-// adapters (40 million bf16 parameters, 8-bit states 92.3 -> 68.3 us; 20 million
-// 58.8 -> 36.5), and a workgroup finds its tensor by two scalar loads where a
-// Batch is searched (65 norms 4.4 -> 3.8 us, 45 million in 7 tensors 77.1 -> 74.4).
+// adapters, and a workgroup finds its tensor by two scalar loads where a Batch is
+// searched (bf16 parameters, 8-bit states, a Batch and a Flat in turn: 40 million
+// in 448 tensors 102 and 80 us a step, 20 million in 448 60 and 40, 45 million in 7
+// 89 and 88; 65 norms 7 either way, the host's time).
 template <bool BITS8>
 struct Flat {
   static constexpr int kMost = 480;
@@ -226,9 +227,11 @@ __device__ __forceinline__ uint2 encode_state(const float x[8], const uint32_t u
   return make_uint2(top_bytes(c[0], c[1], c[2], c[3]), top_bytes(c[4], c[5], c[6], c[7]));
 }
 
-// Correctly rounded square roots.  One step of v / sqrt(v) from the hardware's
-// reciprocal root settles the rounding where neither the root's square nor its
-// remainder leaves fp32; the rest takes the library's function.
+// Square roots, off by half a step but for a few values in 2^23: one Newton step
+// on the remainder, s + (v - s s) q / 2 with s = v q and q the hardware's
+// reciprocal root, rounds wrongly only where q itself is off (by one step: 1 to 3
+// of the 2^23 significands, then by one step of the root).  Where the root's
+// square or its remainder could leave fp32 the library's function takes over.
 __device__ __forceinline__ void roots8(const float v[8], float r[8]) {
   float lo = v[0], hi = v[0];
 #pragma unroll

@@ -246,7 +246,7 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_small_kernel(Fp8In x, Fp8In w,
 // LDS after it.  There are no branches in a step (a refill past the last block
 // repeats it, never read): with one, the compiler sinks the additions past it
 // and keeps every block sum of the step in registers.  28672 x 8192 x 8192:
-// 2950 -> 1630 us (2.36 PFLOP/s) against the plain two-stage loop on 128 x 128
+// 2950 -> 1650 us (2.33 PFLOP/s) against the plain two-stage loop on 128 x 128
 // tiles, bitwise the same sums; the matrix cores are busy 62% of the cycles at
 // a clock that the load holds to 1.55 GHz.  32 x 32 x 64 MFMAs took the same
 // time.

@@ -368,7 +368,10 @@ int nf4_fp8_quantize(const void *x, int x_dtype, int64_t ldx, const nf4_fp8_tens
  * Y = X W^T: X an 8-bit tensor with block_rows 1 [M, K] in either format, W one
  * with block_rows 128 [N, K] in e4m3; Y device [M, N] in y_dtype.  Each
  * block of 128 products is summed in fp32, multiplied by the two scales' fp32
- * product and added in fp32; Y is rounded once.  A bf16 Y is formed on the fp8
+ * product and added in fp32; Y is rounded once.  (A product of scales below
+ * 2^-126 is a subnormal number: its rounding is worth at most 2^-125 of Y a
+ * block, 2^-118 with an e5m2 X.  One of 2^128 or more makes the block an infinity, or a NaN where its
+ * sum is zero.)  A bf16 Y is formed on the fp8
  * matrix cores, which keep 13 bits below the largest of the products they add
  * at once (about 1e-5 of a block's sum); an fp32 Y on the bf16 matrix cores,
  * with every product and sum in fp32.  Any
