@@ -512,7 +512,13 @@ void launch_any(const Fp8In &x, const Fp8In &w, void *y, hipStream_t s) {
     // 6.7, 8.3, 10.7; 8192 x 4096 11.8, 8.9, 12.4, 20.0; 28672 x 8192 67.7, 57.8,
     // 47.2, 45.4; with 3 and 4: 11008 x 4096 11.8 and 12.9; with 5, 6, 8: 20480 x
     // 4096 17.1, 19.0, 21.9, 24576 x 4096 28.6, 18.6, 21.8; with 7 and 8: 28672 x
-    // 8192 43.0 and 45.6).
+    // 8192 43.0 and 45.6).  The waves and the blocks in flight beside them, here
+    // and for up to 64 rows, were taken from runs at one or two of those widths
+    // each.  Among 1, 2, 4 blocks and 4, 8, 12, 16 waves at K = 2048, 4096, 8192
+    // they are the fastest or within 9% of it for bf16 outputs (16 x 20416 x 4096
+    // 19.1 us, 17.5 with 1 and 12; 16 x 32704 x 4096 27.1, the fastest), and within
+    // 19% for fp32 ones, where 12 or 16 waves lead from five row groups on and with
+    // two groups of X (16 x 20416 x 4096 22.7 and 19.5).
     switch ((N + 16 * 256 - 1) / (16 * 256)) {
       case 1: launch_small<1, 1, 4, 8, E5M2, F32OUT, VEC>(x, w, y, s); break;
       case 2: launch_small<1, 2, 4, 8, E5M2, F32OUT, VEC>(x, w, y, s); break;
